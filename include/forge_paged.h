@@ -442,7 +442,9 @@ FORGE_API int forge_paged_prefill(const forge_tensor *q, const forge_tensor *k_c
  *
  * Arithmetic: bf16 products with fp32 accumulation on the tensor cores,
  * softmax in fp32, the weights in the P V product as bf16 high + low parts
- * (about 16 significant bits; with f32 out a third part, 24 bits).  The result
+ * (about 16 significant bits; with f32 out a third part, 24 bits).  One sum on
+ * the tensor cores takes at most 640 products of 16 tokens (384 with f32 out),
+ * however long the context; sums are joined in fp32.  The result
  * depends on the inputs and the GPU's SM count alone: it repeats bit for bit.
  * Enqueues one kernel, or two when contexts are long enough to be cut over the
  * SMs.  The cut rows live in the library-owned scratch of the stream (at most

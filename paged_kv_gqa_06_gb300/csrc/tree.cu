@@ -49,6 +49,19 @@
 // Two CTAs share an SM in the one-tile modes (256 TMEM columns each), so one
 // CTA's softmax overlaps the other's MMAs.
 //
+// Each addition of an MMA to O drops bits of the sum so far, in one direction,
+// so the error of one accumulation grows with its length: less than 2^-23 of a
+// sum that grows evenly, 2^-24 of the result for each.  Over a share of 16384
+// tokens (weights just above 0.5, V of one sign) it was 7.6e-4 on results near
+// 7.5, and bf16 out was off by 0.0164.  So a segment's O starts anew after
+// sum_stages() stages; what it held goes to a side sum in the scratch (the slot
+// that the segment's piece takes when it is cut), added in fp32 with the
+// maxima's factors.  The bound is 3.1e-4 of |out| < 8 for bf16 out, whose own
+// rounding is 1.56e-2, and 1.8e-4 for fp32 out; measured 0.0159 and 1.5e-4, at any
+// length.  Segments that long are those of large batches; 32 sequences of 16384
+// tokens, 12 / 24 nodes, 8 KV heads of 4: 336 / 349 us with bf16 out (334 / 347 in
+// one sum), 381 / 531 us with fp32 out (376 / 530).
+//
 // Masked positions: only the stages that reach past P take the masked path.
 // There the V rows of nodes may hold infinities or NaN that some rows do not
 // see, and 0 * inf is NaN: such elements are set to zero in shared memory and
@@ -97,6 +110,12 @@ struct Cfg {
   static constexpr int kQTile = kBoxes * kRows * 128;
   static constexpr int kStage = kBoxes * kTok * 128;       // K or V of a stage
   static constexpr int kRing = kPair && D == 128 ? 2 : 4;  // stages of the K ring, and of the V ring
+  // Stages of one accumulation of O, at most: 640 products of 16 tokens for
+  // bf16 out, 384 for fp32 out, of a weight's parts 2 and 3 (in the halves of a
+  // tile 1 and 2).
+  __host__ __device__ static constexpr int sum_stages(bool half) {
+    return MODE >= kFull32 ? (half ? 48 : 32) : (half ? 160 : 80);
+  }
   static constexpr int kSWidth = MODE == kFull32 ? 96 : 64;  // TMEM columns of an S buffer
   static constexpr int kTmem = kPair ? 256 : 512;
   __host__ __device__ static constexpr int o_col(int t) { return 128 * t; }
@@ -333,6 +352,81 @@ __device__ __forceinline__ uint32_t seen_bits(uint64_t first, const int64_t* mas
 // bf16 pairs: all-ones mask in each half whose exponent is all ones.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); }
 
+// 32 columns of a row's O.  Where the weights' parts lie in the tile's halves
+// (`half`, all of the tile's threads call this), the low parts' O is added in
+// the thread with the high parts', over `add` in shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void read_o(uint32_t taddr, bool half, bool upper, float4* add, uint32_t (&v)[32]) {
+  tc::ld_32x32b_x32(taddr, v);
+  tc::wait_ld();
+  if constexpr (PAIR) {
+    if (half) {
+      if (upper) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          add[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                               __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+      }
+      named_barrier(1, kRows);
+      if (!upper) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 x = add[e];
+          v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) + x.x);
+          v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) + x.y);
+          v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) + x.z);
+          v[4 * e + 3] = __float_as_uint(__uint_as_float(v[4 * e + 3]) + x.w);
+        }
+      }
+      named_barrier(1, kRows);
+    }
+  }
+}
+// A row of a piece or of a side sum lies as [4-dim group][row], so that a
+// warp's 32 rows store together.
+template <int ITEM_ROWS>
+__device__ __forceinline__ void store_piece(float4* po, int c4, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    po[(8 * c4 + e) * ITEM_ROWS] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                               __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+}
+template <int ITEM_ROWS>
+__device__ __forceinline__ void add_piece(const float4* po, int c4, float f, uint32_t (&v)[32]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 x = po[(8 * c4 + e) * ITEM_ROWS];
+    v[4 * e] = __float_as_uint(fmaf(x.x, f, __uint_as_float(v[4 * e])));
+    v[4 * e + 1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(v[4 * e + 1])));
+    v[4 * e + 2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(v[4 * e + 2])));
+    v[4 * e + 3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(v[4 * e + 3])));
+  }
+}
+// What a side sum against `from` is worth against `to` (-inf: nothing seen).
+__device__ __forceinline__ float side_factor(float from, float to) {
+  return fast_exp2(from - (to == -INFINITY ? 0.f : to));
+}
+// O into the side sum at `po` (whose maximum is kept in `ml`), before the next
+// products start it anew.  `mine`: this thread keeps the row.  (Not inlined:
+// rarely called, its registers would be spilled in the loop over the stages.)
+template <int D, int ITEM_ROWS, bool PAIR>
+__device__ __noinline__ void sum_aside(uint32_t tcol, bool half, bool upper, bool mine, bool first, float m,
+                                       float4* add, float4* po, float2* ml) {
+  tc::fence_after_sync();
+  const float f = mine && !first ? side_factor(ml->x, m) : 0.f;
+#pragma unroll 1
+  for (int c4 = 0; c4 < D / 32; ++c4) {
+    uint32_t v[32];
+    read_o<PAIR>(tcol + 32 * c4, half, upper, add, v);
+    if (mine) {
+      if (!first) add_piece<ITEM_ROWS>(po, c4, f, v);
+      store_piece<ITEM_ROWS>(po, c4, v);
+    }
+    __syncwarp();
+  }
+  if (mine) ml->x = m;
+}
+
 // ------------------------------------------------------------ main kernel
 template <int D, int G, int MODE>
 __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 2 : 1)
@@ -544,7 +638,10 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
     do {
       const int ns = k.st1 - k.st0, nt = k.tiles();
       const bool half = MODE == kHalf32 || (MODE == kOneTile && k.rows() <= 64);
+      int fresh = 0;  // the next stage that starts O anew
       for (int i = 0; ok && i < ns; ++i, ++ring) {
+        const bool add = i != fresh;
+        if (!add) fresh += C::sum_stages(half);
         ok = ok && mbar_wait(bars + C::kVFull + ring % C::kRing, (ring / C::kRing) & 1, p.err);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
@@ -563,13 +660,13 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
               if (half) {
                 // 8 columns hold high (rows 0-63) and low parts (64-127); the
                 // third parts follow behind 32 columns
-                tc::mma_bf16_ts(dout, pc + 8 * s, bd, IDESC_O, i > 0 || s > 0);
+                tc::mma_bf16_ts(dout, pc + 8 * s, bd, IDESC_O, add || s > 0);
                 if constexpr (MODE == kHalf32) tc::mma_bf16_ts(dout, pc + 32 + 8 * s, bd, IDESC_O, true);
               } else {
                 // high parts in 8 columns of their chunk of 32, low parts 16
                 // columns on, third parts behind the 64 columns
                 const uint32_t hi = pc + 32 * (s >> 1) + 8 * (s & 1);
-                tc::mma_bf16_ts(dout, hi, bd, IDESC_O, i > 0 || s > 0);
+                tc::mma_bf16_ts(dout, hi, bd, IDESC_O, add || s > 0);
                 tc::mma_bf16_ts(dout, hi + 16, bd, IDESC_O, true);
                 if constexpr (MODE == kFull32) tc::mma_bf16_ts(dout, pc + 64 + 8 * s, bd, IDESC_O, true);
               }
@@ -608,130 +705,149 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
         const int64_t* mask = p.mask + static_cast<int64_t>(k.s.q0 + (ok ? node : 0)) * p.m_st;
         const uint64_t first_word = static_cast<uint64_t>(__ldg(mask));
         float m_used = -INFINITY, l = 0.f;  // max the weights are taken against; row sum
-        for (int i = 0; i < ns; ++i, ++at) {
-          const int buf = at & 1;
-          mbar_wait(bars + C::kSFull + 2 * t + buf, (at >> 1) & 1, p.err);
-          tc::fence_after_sync();
-          const int t0 = (k.st0 + i) * kTok;
-          const bool edge = t0 + kTok > P;  // the stage reaches the nodes (or the end)
-          if (live) {
-            const uint32_t sc = trow + C::s_col(t, buf);
-            uint32_t v[kTok];
-            tc::ld_32x32b_x32(sc, *reinterpret_cast<uint32_t(*)[32]>(v));
-            tc::ld_32x32b_x32(sc + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-            tc::wait_ld();
-            float mx;
-            float mul = scale;
-            if (edge || scale < 0.f) {
-              // scaled and masked here; a negative scale also turns the maximum
-              mul = 1.f;
-              mx = -INFINITY;
+        // this row of the piece, and of the side sum until then, and its (max,
+        // sum); this thread alone writes and reads them here
+        auto piece = [&] {
+          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg > 0);
+          return reinterpret_cast<float4*>(p.ws_o) + slot * (C::kItemRows * (D / 4)) + t * kRows + rr;
+        };
+        auto piece_ml = [&] {
+          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg > 0);
+          return reinterpret_cast<float2*>(p.ws_ml) + slot * C::kItemRows + t * kRows + rr;
+        };
+        auto add_at = [&] { return reinterpret_cast<float4*>(sm + C::kAdd) + (r & 63) * (kAddRow / 4); };
+        for (int i0 = 0, i1; i0 < ns; i0 = i1) {  // runs of one accumulation of O
+          i1 = min(ns, i0 + C::sum_stages(half));
+          if (i0 > 0 && (live || half)) {
+            mbar_wait(bars + C::kPvDone + 2 * t + ((at - 1) & 1), ((at - 1) >> 1) & 1, p.err);
+            sum_aside<D, C::kItemRows, C::kPair>(trow + C::o_col(t), half, upper, ok && !upper,
+                                                 i0 == C::sum_stages(half), m_used, add_at(), piece(), piece_ml());
+          }
+          for (int i = i0; i < i1; ++i, ++at) {
+            const int buf = at & 1;
+            mbar_wait(bars + C::kSFull + 2 * t + buf, (at >> 1) & 1, p.err);
+            tc::fence_after_sync();
+            const int t0 = (k.st0 + i) * kTok;
+            const bool edge = t0 + kTok > P;  // the stage reaches the nodes (or the end)
+            if (live) {
+              const uint32_t sc = trow + C::s_col(t, buf);
+              uint32_t v[kTok];
+              tc::ld_32x32b_x32(sc, *reinterpret_cast<uint32_t(*)[32]>(v));
+              tc::ld_32x32b_x32(sc + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+              tc::wait_ld();
+              float mx;
+              float mul = scale;
+              if (edge || scale < 0.f) {
+                // scaled and masked here; a negative scale also turns the maximum
+                mul = 1.f;
+                mx = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t bits = edge ? seen_bits(first_word, mask, p.W, t0 + 32 * h, P, k.s.L) : 0xffffffffu;
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) {
+                    const float x = (bits >> c) & 1u ? __uint_as_float(v[32 * h + c]) * scale : -INFINITY;
+                    v[32 * h + c] = __float_as_uint(x);
+                    mx = fmaxf(mx, x);
+                  }
+                }
+              } else {
+                float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kTok; c += 8) {
+                  m0 = fmax3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                  m1 = fmax3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                  m2 = fmax3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                  m3 = fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+                }
+                mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale;
+              }
+              const float m_new = fmaxf(m_used, mx);
+              const bool need = ok && m_new > m_used + kRescaleSlack;
+              const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;  // 0 at the row's first seen token
+              if (need) {
+                l *= alpha;
+                m_used = m_new;
+              }
+              if (i > i0 && __any_sync(kFullMask, need)) {
+                mbar_wait(bars + C::kPvDone + 2 * t + ((at - 1) & 1), ((at - 1) >> 1) & 1, p.err);  // O stands still
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int c4 = 0; c4 < D / 32; ++c4) {
+                  uint32_t o[32];
+                  tc::ld_32x32b_x32(trow + C::o_col(t) + 32 * c4, o);
+                  tc::wait_ld();
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                  tc::st_32x32b_x32(trow + C::o_col(t) + 32 * c4, o);
+                }
+              }
+              const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: every weight is 2^-inf
+              const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(-m_ref, -m_ref);
+              float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t bits = edge ? seen_bits(first_word, mask, p.W, t0 + 32 * h, P, k.s.L) : 0xffffffffu;
+                uint32_t hi[16], lo[16], lo2[16];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const float x = (bits >> c) & 1u ? __uint_as_float(v[32 * h + c]) * scale : -INFINITY;
-                  v[32 * h + c] = __float_as_uint(x);
-                  mx = fmaxf(mx, x);
+                for (int e = 0; e < 16; ++e) {
+                  const float2 y = ffma2(make_float2(__uint_as_float(v[32 * h + 2 * e]), __uint_as_float(v[32 * h + 2 * e + 1])),
+                                         mul2, nm2);
+                  const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                  l2[e & 1] = fadd2(l2[e & 1], w);
+                  split_bf16x2(w.x, w.y, hi[e], lo[e]);
+                  if constexpr (MODE >= kFull32) {
+                    const float r0 = w.x - bf16lo(hi[e]) - bf16lo(lo[e]), r1 = w.y - bf16hi(hi[e]) - bf16hi(lo[e]);
+                    lo2[e] = pack_bf16x2(r0, r1);
+                  }
+                }
+                if (half) {
+                  if constexpr (MODE == kHalf32) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) lo2[e] = upper ? 0u : lo2[e];
+                    tc::st_32x32b_x16(sc + 32 + 16 * h, lo2);
+                  }
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) hi[e] = upper ? lo[e] : hi[e];
+                  tc::st_32x32b_x16(sc + 16 * h, hi);
+                } else {
+                  tc::st_32x32b_x16(sc + 32 * h, hi);
+                  tc::st_32x32b_x16(sc + 32 * h + 16, lo);
+                  if constexpr (MODE == kFull32) tc::st_32x32b_x16(sc + 64 + 16 * h, lo2);
                 }
               }
-            } else {
-              float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < kTok; c += 8) {
-                m0 = fmax3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                m1 = fmax3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-                m2 = fmax3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
-                m3 = fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
-              }
-              mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale;
+              l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
+              tc::wait_st();
             }
-            const float m_new = fmaxf(m_used, mx);
-            const bool need = ok && m_new > m_used + kRescaleSlack;
-            const float alpha = need ? fast_exp2(m_used - m_new) : 1.f;  // 0 at the row's first seen token
-            if (need) {
-              l *= alpha;
-              m_used = m_new;
-            }
-            if (i > 0 && __any_sync(kFullMask, need)) {
-              mbar_wait(bars + C::kPvDone + 2 * t + ((at - 1) & 1), ((at - 1) >> 1) & 1, p.err);  // O stands still
-              tc::fence_after_sync();
-#pragma unroll 1
-              for (int c4 = 0; c4 < D / 32; ++c4) {
-                uint32_t o[32];
-                tc::ld_32x32b_x32(trow + C::o_col(t) + 32 * c4, o);
-                tc::wait_ld();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                tc::st_32x32b_x32(trow + C::o_col(t) + 32 * c4, o);
-              }
-            }
-            const float m_ref = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: every weight is 2^-inf
-            const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(-m_ref, -m_ref);
-            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t hi[16], lo[16], lo2[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 y = ffma2(make_float2(__uint_as_float(v[32 * h + 2 * e]), __uint_as_float(v[32 * h + 2 * e + 1])),
-                                       mul2, nm2);
-                const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                l2[e & 1] = fadd2(l2[e & 1], w);
-                split_bf16x2(w.x, w.y, hi[e], lo[e]);
-                if constexpr (MODE >= kFull32) {
-                  const float r0 = w.x - bf16lo(hi[e]) - bf16lo(lo[e]), r1 = w.y - bf16hi(hi[e]) - bf16hi(lo[e]);
-                  lo2[e] = pack_bf16x2(r0, r1);
+            if (edge && t == 0) {
+              // V rows of the nodes without their infinities and NaN, zeros
+              // past the end (the slots there may hold anything)
+              const int slot = (ring + i) % C::kRing;
+              mbar_wait(bars + C::kVFull + slot, ((ring + i) / C::kRing) & 1, p.err);
+              unsigned char* vst = sm + C::kV + slot * C::kStage;
+              const int z0 = max(P - t0, 0);
+              for (int idx = r; idx < (kTok - z0) * C::kBoxes * 8; idx += kRows) {
+                const int vr = z0 + idx / (C::kBoxes * 8), rest = idx % (C::kBoxes * 8);
+                uint4* at4 = reinterpret_cast<uint4*>(vst + (rest >> 3) * kTok * 128 + vr * 128 + (rest & 7) * 16);
+                if (t0 + vr >= k.s.L) {
+                  *at4 = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                  uint4 x = *at4;
+                  const uint32_t b0 = nonfinite2(x.x), b1 = nonfinite2(x.y), b2 = nonfinite2(x.z), b3 = nonfinite2(x.w);
+                  if (b0 | b1 | b2 | b3) {
+                    *at4 = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
+                    *bad_v = 1;
+                  }
                 }
               }
-              if (half) {
-                if constexpr (MODE == kHalf32) {
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) lo2[e] = upper ? 0u : lo2[e];
-                  tc::st_32x32b_x16(sc + 32 + 16 * h, lo2);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) hi[e] = upper ? lo[e] : hi[e];
-                tc::st_32x32b_x16(sc + 16 * h, hi);
-              } else {
-                tc::st_32x32b_x16(sc + 32 * h, hi);
-                tc::st_32x32b_x16(sc + 32 * h + 16, lo);
-                if constexpr (MODE == kFull32) tc::st_32x32b_x16(sc + 64 + 16 * h, lo2);
-              }
+              fence_proxy_async_smem();  // before the tensor cores read it
             }
-            l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
-            tc::wait_st();
+            // (every warp sees every phase of a barrier, in order: a parity tells
+            // a phase only from its neighbours)
+            if (i > 0) mbar_wait(bars + C::kPvDone + 2 * t + ((at - 1) & 1), ((at - 1) >> 1) & 1, p.err);
+            tc::fence_before_sync();  // P in TMEM before the arrival
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + C::kPFull + 2 * t + buf);
           }
-          if (edge && t == 0) {
-            // V rows of the nodes without their infinities and NaN, zeros
-            // past the end (the slots there may hold anything)
-            const int slot = (ring + i) % C::kRing;
-            mbar_wait(bars + C::kVFull + slot, ((ring + i) / C::kRing) & 1, p.err);
-            unsigned char* vst = sm + C::kV + slot * C::kStage;
-            const int z0 = max(P - t0, 0);
-            for (int idx = r; idx < (kTok - z0) * C::kBoxes * 8; idx += kRows) {
-              const int vr = z0 + idx / (C::kBoxes * 8), rest = idx % (C::kBoxes * 8);
-              uint4* at4 = reinterpret_cast<uint4*>(vst + (rest >> 3) * kTok * 128 + vr * 128 + (rest & 7) * 16);
-              if (t0 + vr >= k.s.L) {
-                *at4 = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                uint4 x = *at4;
-                const uint32_t b0 = nonfinite2(x.x), b1 = nonfinite2(x.y), b2 = nonfinite2(x.z), b3 = nonfinite2(x.w);
-                if (b0 | b1 | b2 | b3) {
-                  *at4 = make_uint4(x.x & ~b0, x.y & ~b1, x.z & ~b2, x.w & ~b3);
-                  *bad_v = 1;
-                }
-              }
-            }
-            fence_proxy_async_smem();  // before the tensor cores read it
-          }
-          // (every warp sees every phase of a barrier, in order: a parity tells
-          // a phase only from its neighbours)
-          if (i > 0) mbar_wait(bars + C::kPvDone + 2 * t + ((at - 1) & 1), ((at - 1) >> 1) & 1, p.err);
-          tc::fence_before_sync();  // P in TMEM before the arrival
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + C::kPFull + 2 * t + buf);
         }
 
         // ---- this segment's rows, after its last P V
@@ -742,39 +858,14 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that saw nothing gives zeros
         OutT* dst = reinterpret_cast<OutT*>(p.out) + static_cast<int64_t>(k.s.q0 + node) * p.o_st +
                     static_cast<int64_t>(head) * p.o_sh;
-        // a piece's rows: [4-dim group][row], so that a warp's 32 rows store together
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (seg > 0);
-        float4* po = reinterpret_cast<float4*>(p.ws_o) + slot * (C::kItemRows * (D / 4)) + t * kRows + rr;
         if (live || half) {
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 32; ++c4) {
             uint32_t v[32];
-            tc::ld_32x32b_x32(trow + C::o_col(t) + 32 * c4, v);
-            tc::wait_ld();
-            if constexpr (C::kPair) {
-              if (half) {  // the low parts' O to the thread with the high parts'
-                float4* add = reinterpret_cast<float4*>(sm + C::kAdd) + (r & 63) * (kAddRow / 4);
-                if (upper) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    add[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                         __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                }
-                named_barrier(1, kRows);
-                if (!upper) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    const float4 x = add[e];
-                    v[4 * e] = __float_as_uint(__uint_as_float(v[4 * e]) + x.x);
-                    v[4 * e + 1] = __float_as_uint(__uint_as_float(v[4 * e + 1]) + x.y);
-                    v[4 * e + 2] = __float_as_uint(__uint_as_float(v[4 * e + 2]) + x.z);
-                    v[4 * e + 3] = __float_as_uint(__uint_as_float(v[4 * e + 3]) + x.w);
-                  }
-                }
-                named_barrier(1, kRows);
-              }
-            }
+            read_o<C::kPair>(trow + C::o_col(t) + 32 * c4, half, upper, add_at(), v);
             if (upper) continue;
+            if (ok && ns > C::sum_stages(half))
+              add_piece<C::kItemRows>(piece(), c4, side_factor(piece_ml()->x, m_used), v);
             if (fix && ok) {
               // the infinities and NaN of the nodes this row sees
               const int a = max(P, k.st0 * kTok), z = min(k.s.L, k.st1 * kTok);
@@ -795,17 +886,11 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
             if (ok) {
               if (whole)
                 store_row32(dst + 32 * c4, v, inv);
-              else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  po[(8 * c4 + e) * C::kItemRows] =
-                      make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                  __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-              }
+              else
+                store_piece<C::kItemRows>(piece(), c4, v);
             }
           }
-          if (ok && !whole && !upper)
-            reinterpret_cast<float2*>(p.ws_ml)[slot * C::kItemRows + t * kRows + rr] = make_float2(m_used, l);
+          if (ok && !whole && !upper) *piece_ml() = make_float2(m_used, l);
         }
         tc::fence_before_sync();  // O read before the next segment's first P V
         if (!whole && k.st0 == 0 && threadIdx.x == 0) {
@@ -1089,7 +1174,6 @@ TreePlan plan_tree(int64_t T, int64_t B, int64_t Hkv, int64_t MB, int G, int D, 
   const int64_t most = r.split ? items * (stages + item_cost(static_cast<int>(rows))) / r.min_share : items;
   r.grid = static_cast<int>(most < 1 ? 1 : most > resident ? resident : most);
   r.grid = r.grid > kMaxShares ? kMaxShares : r.grid;
-  r.split = r.split && r.grid > 1;
   r.merge_grid = 4 * num_sms;
   const int64_t pieces = 2ll * r.grid;                             // two a CTA
   r.o_bytes = static_cast<size_t>(pieces * rows) * D * 4;
