@@ -386,7 +386,9 @@ constexpr int kMoveBlock = 512;     // rows translated at a time
 constexpr int kMoveRing = 1024;     // translated rows held
 constexpr int kMoveTotals = 4;      // totals a thread moves per round
 constexpr uint32_t kNoMove = 0xffffffffu;
-static_assert(kMoveRing >= kMoveBlock + kMoveStages * kMoveRows, "rows in flight keep their addresses");
+// A fast thread translates for round r + kMoveStages while a slow one still
+// writes the rows of round r: kMoveStages + 1 rounds, and what a block adds.
+static_assert(kMoveRing >= kMoveBlock - 1 + (kMoveStages + 1) * kMoveRows, "rows in flight keep their addresses");
 
 template <int CHUNKS>               // 16-byte chunks of a row; 0: p.D / 8
 __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactParams p, int cluster) {
