@@ -151,7 +151,7 @@ __device__ __forceinline__ int ld_nc_keep(const int32_t* ptr) {
 }
 
 __device__ __forceinline__ int checked_length(const DecodeParams& p, int b, bool report) {
-  int L = __ldg(p.context_lens + b);
+  int L = p.context_lens[b];  // an ordinary load: the grid before may have written it beside this one
   const int Lmax = p.MB * kBlockSize;
   if (L < 0 || L > Lmax) {
     if (report) record_error(p.err, kDevErrLength);

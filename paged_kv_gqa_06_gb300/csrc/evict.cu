@@ -11,9 +11,16 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// All of these kernels start while the grid before them may still run, so what
+// that grid can have written (totals, lists, lengths, tables) is read with
+// ordinary loads after the wait, never with non-coherent ones, whose data must
+// not change while a kernel lives.
+
 // Length of sequence b, clamped to [0, most]; a length outside is recorded.
+// AHEAD: read before the wait, past L1.
+template <bool AHEAD = false>
 __device__ __forceinline__ int length_of(const int32_t* lens, int b, int most, int* err, bool report) {
-  int L = __ldg(lens + b);
+  int L = AHEAD ? __ldcg(lens + b) : lens[b];
   if (L < 0 || L > most) {
     if (report) record_error(err, kDevErrLength);
     L = L < 0 ? 0 : most;
@@ -40,7 +47,7 @@ template <int G>
 __global__ void __launch_bounds__(kAccThreads, G <= 4 ? 8 : 5) accumulate_weights_kernel(const WeightsParams p) {
   griddep_launch_dependents();
   const int g = blockIdx.y, b = blockIdx.z;
-  int L = length_of(p.context_lens, b, p.MB * kBlockSize, nullptr, false);  // recorded by the decode
+  int L = length_of<true>(p.context_lens, b, p.MB * kBlockSize, nullptr, false);  // recorded by the decode
   if (L > p.S) {
     if (g == 0 && blockIdx.x == 0 && threadIdx.x == 0) record_error(p.err, kDevErrLength);
     L = p.S;
@@ -57,7 +64,7 @@ __global__ void __launch_bounds__(kAccThreads, G <= 4 ? 8 : 5) accumulate_weight
   float* dst = p.weights + b * p.w_sb + g * p.w_sh + t0;
   float w[kAccEach];
 #pragma unroll
-  for (int e = 0; e < kAccEach; ++e) w[e] = t0 + e * kAccThreads < L ? dst[e * kAccThreads] : 0.f;
+  for (int e = 0; e < kAccEach; ++e) w[e] = t0 + e * kAccThreads < L ? __ldcg(dst + e * kAccThreads) : 0.f;
   griddep_wait();  // the decode that writes the logits is complete
   float2 nm[G];
 #pragma unroll
@@ -97,6 +104,15 @@ __global__ void __launch_bounds__(kAccThreads, G <= 4 ? 8 : 5) accumulate_weight
 }
 
 // --------------------------------------------------------------- selection
+// An ordinary load that the compiler leaves where it is.  (Merged with the
+// shared-memory side of the choice it is used in, it took the kernel past 32
+// registers a thread and one CTA off each SM: 256 lists 13.6 -> 14.9 us.)
+__device__ __forceinline__ float ld_here(const float* ptr) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(ptr) : "memory");
+  return v;
+}
+
 // Weights as unsigned keys of the same order: NaN as -infinity, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float x) {
   if (x != x) x = -INFINITY;
@@ -193,7 +209,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   const int run0 = lo + static_cast<int>(min(static_cast<int64_t>(rank) * share, static_cast<int64_t>(hi) - lo));
   const int run = min(share, hi - run0);
   const bool held = run <= kSelCap;
-  auto key = [&](int i) { return held ? keys[i] : weight_key(__ldg(w + run0 + i)); };
+  auto key = [&](int i) { return held ? keys[i] : weight_key(ld_here(w + run0 + i)); };
   // counts `digit` (negative: none); a warp of equal digits (totals that are
   // all alike) counts once, not 32 times in turn
   auto count_digit = [&](int* hist, int digit) {
@@ -220,7 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 #pragma unroll
       for (int e = 0; e < kSelAhead; ++e) {
         const int i = i0 + e * kSelThreads + tid;
-        x[e] = i < run ? __ldg(w + run0 + i) : 0.f;
+        x[e] = i < run ? w[run0 + i] : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < kSelAhead; ++e) {
@@ -399,9 +415,9 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
   const int rank = static_cast<int>(cluster_rank()), tid = threadIdx.x;
   const int g = blockIdx.x / cluster, b = blockIdx.y, plane = blockIdx.z;
   const bool first = g == 0 && plane == 0 && rank == 0 && tid == 0;
-  const int L = __ldg(p.context_lens + b);
-  const int n = __ldg(p.kept_lens + b);
-  const int d = p.dst_start ? __ldg(p.dst_start + b) : 0;
+  const int L = p.context_lens[b];
+  const int n = p.kept_lens[b];
+  const int d = p.dst_start ? p.dst_start[b] : 0;
   if (L < 0 || L > p.MB * kBlockSize) {
     if (first) record_error(p.err, kDevErrLength);
     return;
@@ -419,8 +435,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
   };
   // source of entry i, -1 when it breaks the rules
   auto entry = [&](int i) -> int {
-    const int s = __ldg(list + i);
-    const int before = i > 0 ? __ldg(list + i - 1) : -1;
+    const int s = list[i];
+    const int before = i > 0 ? list[i - 1] : -1;
     if (s >= d + i && s < L && s > before) return s;
     record_error(p.err, kDevErrKept);
     return -1;
@@ -461,7 +477,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
   const int per = min(kMoveRows, kMoveChunks / chunks);  // rows of a round and CTA
   const int rounds = (n + cluster * per - 1) / (cluster * per);
   auto slot_of = [&](int t) -> uint32_t {
-    const int blk = __ldg(table + t / kBlockSize);
+    const int blk = table[t / kBlockSize];
     if (static_cast<unsigned>(blk) < static_cast<unsigned>(p.NB))
       return static_cast<uint32_t>(blk) * kBlockSize + t % kBlockSize;
     record_error(p.err, kDevErrBlockId);

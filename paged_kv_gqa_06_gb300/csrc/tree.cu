@@ -159,9 +159,9 @@ struct Seq {
 template <int G, int IR>  // IR: rows of an item
 __device__ __forceinline__ Seq seq_of(const TreeParams& p, int b) {
   Seq s;
-  s.q0 = __ldg(p.query_start + b);
-  const int64_t n = static_cast<int64_t>(__ldg(p.query_start + b + 1)) - s.q0;
-  s.L = __ldg(p.context_lens + b);
+  s.q0 = p.query_start[b];
+  const int64_t n = static_cast<int64_t>(p.query_start[b + 1]) - s.q0;
+  s.L = p.context_lens[b];
   const bool ok = n > 0 && s.q0 >= 0 && s.q0 + n <= p.T && s.L <= p.MB * kBlockSize && n <= s.L && n <= 64ll * p.W;
   s.n = ok ? static_cast<int>(n) : 0;
   s.stages = ok ? (s.L + kTok - 1) / kTok : 0;
@@ -331,7 +331,7 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t (
 // P, the node's bits from P, zeros from L.
 // `first` is the row's first mask word, read ahead.
 __device__ __forceinline__ uint32_t seen_bits(uint64_t first, const int64_t* mask, int words, int t, int P, int L) {
-  auto word = [&](int w) { return w == 0 ? first : static_cast<uint64_t>(__ldg(mask + w)); };
+  auto word = [&](int w) { return w == 0 ? first : static_cast<uint64_t>(mask[w]); };
   const int j = t - P;  // node index of position t
   uint32_t bits;
   if (j <= -32) {
@@ -478,12 +478,15 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
     // would hold it until this grid is complete.
     griddep_launch_dependents();
   }
-  griddep_wait();  // the lengths, tables, q and cache below are the previous grid's results
+  // The lengths, tables, masks, q and cache below are the previous grid's
+  // results: read after the wait, with ordinary loads (that grid may have run
+  // beside this one, and a non-coherent load wants unchanging data).
+  griddep_wait();
   if (warp == 0) {
     if (blockIdx.x == 0) {  // the rules for every sequence, checked once
       int code = 0;
       for (int b = lane; b < p.B; b += 32) {
-        const int s0 = __ldg(p.query_start + b), s1 = __ldg(p.query_start + b + 1), L = __ldg(p.context_lens + b);
+        const int s0 = p.query_start[b], s1 = p.query_start[b + 1], L = p.context_lens[b];
         const int64_t n = static_cast<int64_t>(s1) - s0;
         if (n < 0 || s1 > p.T || (b == 0 && s0 != 0)) code = kDevErrQuery;
         if (n > 0 && (L < 0 || L > p.MB * kBlockSize))
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
       // block ids of 8 stages: lane l holds block l % 4 of stage l / 4
       auto table_group = [&](int st) -> int {
         const int jb = kStageBlks * st + lane;
-        return jb * kBlockSize < k.s.L ? __ldg(row + jb) : -1;
+        return jb * kBlockSize < k.s.L ? row[jb] : -1;
       };
       int ids = table_group(k.st0), ahead = k.st1 - k.st0 > 8 ? table_group(k.st0 + 8) : -1;
       for (int st = k.st0; st < k.st1; ++st, ++ring) {
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
         const bool live = __any_sync(kFullMask, ok);  // a warp past the tree's rows only keeps step
         const int P = k.s.L - k.s.n;
         const int64_t* mask = p.mask + static_cast<int64_t>(k.s.q0 + (ok ? node : 0)) * p.m_st;
-        const uint64_t first_word = static_cast<uint64_t>(__ldg(mask));
+        const uint64_t first_word = static_cast<uint64_t>(*mask);
         float m_used = -INFINITY, l = 0.f;  // max the weights are taken against; row sum
         // this row of the piece, and of the side sum until then, and its (max,
         // sum); this thread alone writes and reads them here
@@ -871,8 +874,8 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
               const int a = max(P, k.st0 * kTok), z = min(k.s.L, k.st1 * kTok);
               for (int x = a; x < z; ++x) {
                 const int j = x - P;
-                if (!((__ldg(mask + (j >> 6)) >> (j & 63)) & 1)) continue;
-                const int blk = __ldg(p.block_tables + static_cast<int64_t>(k.b) * p.bt_sb + x / kBlockSize);
+                if (!((mask[j >> 6] >> (j & 63)) & 1)) continue;
+                const int blk = p.block_tables[static_cast<int64_t>(k.b) * p.bt_sb + x / kBlockSize];
                 if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.NB)) continue;
                 const __nv_bfloat16* vr =
                     p.v_cache + blk * p.vc_sblk + k.g * p.vc_sh + (x % kBlockSize) * D + 32 * c4;

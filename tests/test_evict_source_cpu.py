@@ -44,3 +44,29 @@ def test_the_address_ring_as_built_is_long_enough():
     c = constants(source("evict.cu"))
     assert not any(ring_overwritten(c["kMoveRing"], c["kMoveBlock"], c["kMoveStages"], per)
                    for per in range(1, c["kMoveRows"] + 1))
+
+
+def function(text, name):
+    """The text of a function from its name to the closing brace of its column."""
+    at = re.search(r"^[^\n]*\b%s\([^;]*?\{\n" % name, text, re.M | re.S)
+    return text[at.start(): text.index("\n}\n", at.end())]
+
+
+@pytest.mark.parametrize("name", ["evict.cu", "tree.cu"])
+def test_no_non_coherent_loads_where_the_writer_may_still_run(name):
+    """These kernels start while the grid that writes their lengths, lists and totals may still run; a non-coherent load
+    wants its data unwritten for as long as the kernel lives."""
+    text = re.sub(r"//[^\n]*", "", source(name))
+    assert "__ldg(" not in text and ".nc" not in text and "__restrict__" not in text
+
+
+def test_the_decodes_length_is_no_non_coherent_load():
+    """Lengths may be the kept_lens of a selection that is still running when the decode starts."""
+    assert "__ldg(" not in function(source("decode.cu"), "checked_length")
+
+
+def test_what_the_totals_read_ahead_goes_past_l1():
+    """accumulate_weights reads lengths and totals before its wait: past L1, which may hold older lines."""
+    text = source("evict.cu")
+    ahead = function(text, "accumulate_weights_kernel").split("griddep_wait();  // the decode")[0]
+    assert "__ldcg(" in ahead and "length_of<true>" in ahead
