@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       before.x += cluster_read_int(&sh.counts[0], r);
       before.y += cluster_read_int(&sh.counts[1], r);
     }
+    cluster_arrive();  // this thread's reads of the others' shared memory are done
   }
   auto keep = [&](int i, bool is_above) {
     if (is_above) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   }
   ends();
   if (cluster > 1) {  // no CTA leaves while another reads its shared memory
-    cluster_arrive_relaxed();
+    __syncwarp();
     cluster_wait();
   }
 }

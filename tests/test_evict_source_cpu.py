@@ -70,3 +70,12 @@ def test_what_the_totals_read_ahead_goes_past_l1():
     text = source("evict.cu")
     ahead = function(text, "accumulate_weights_kernel").split("griddep_wait();  // the decode")[0]
     assert "__ldcg(" in ahead and "length_of<true>" in ahead
+
+
+def test_selections_last_barrier_orders_its_reads():
+    """A CTA reads the counts of its cluster's others; its arrival at the barrier that lets them leave must order those
+    reads, which a relaxed one does not."""
+    text = function(source("evict.cu"), "evict_select_kernel")
+    assert "cluster_arrive_relaxed" not in text
+    reads = text.index("cluster_read_int(&sh.counts[1], r)")
+    assert reads < text.index("cluster_arrive();") < text.index("cluster_wait();")
