@@ -432,8 +432,9 @@ FORGE_API int forge_paged_prefill(const forge_tensor *q, const forge_tensor *k_c
  *                  query_start[B] <= T; 0 <= n_b <= min(L_b, 64 W).
  *   tree_mask      int64 [T, W], W >= 1, inner stride 1: bit masks.
  *   scale          finite.
- *   out            f32 or bf16 [T, Hq, D], strides as q; rows outside every
- *                  sequence's range are left as they are.
+ *   out            f32 or bf16 [T, Hq, D], strides as q, rows that do not
+ *                  overlap (FORGE_ERR_SHAPE); rows outside every sequence's
+ *                  range are left as they are.
  * D in {64, 128}, Hq / Hkv in {1, 2, 4, 8}.  A query_start or length that
  * breaks the rules is recorded as FORGE_DEVERR_QUERY / FORGE_DEVERR_LENGTH
  * and that sequence's rows are not written; a bad block id as
@@ -501,7 +502,7 @@ FORGE_API int forge_paged_tree_attention_ex(const forge_tensor *q, const forge_t
  *                  for every sequence: a longer one is recorded as
  *                  FORGE_DEVERR_LENGTH and its totals past S are skipped.
  * Rows of `weights` must not overlap (FORGE_ERR_SHAPE): one of the two strides
- * is at least S, the other covers all of its steps.
+ * is at least S, the other covers all of its steps; nor must rows of `out`.
  * With f32 out the P V product takes the weights at 24 bits, not 16.
  * Scratch, its growth and thread-safety as in forge_paged_gqa_decode
  * (library-owned); it also holds the call's logits, B * Hq * MB * 16 * 4

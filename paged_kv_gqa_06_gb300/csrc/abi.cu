@@ -854,8 +854,8 @@ int weights_split_tokens(int B, int Hkv, int MB, int num_sms) {
   return bps * kBlockSize;
 }
 
-// Rows of `len` elements per (sequence, KV head) that a call writes do not
-// overlap: the dimension with the smaller stride lies inside one step of the
+// Rows of `len` elements of a tensor's first two dimensions that a call writes
+// (per sequence or token, and head) do not overlap: the dimension with the smaller stride lies inside one step of the
 // other.
 int check_rows_apart(const forge_tensor* t, int64_t len) {
   if (t->shape[0] == 0 || t->shape[1] == 0) return FORGE_OK;
@@ -916,6 +916,7 @@ static int tree_attention(const forge_tensor* q, const forge_tensor* k_cache, co
   if (T == 0 || B == 0) return FORGE_OK;
   FORGE_TRY(check_vec16(q, 2));
   FORGE_TRY(check_vec16(out, out->dtype == FORGE_BF16 ? 2 : 4));
+  FORGE_TRY(check_rows_apart(out, D));
   if ((MB > 0 && !block_tables->data) || !context_lens->data || !query_start->data || !tree_mask->data)
     return FORGE_ERR_NULL;
   if (block_tables->stride[1] != 1 || context_lens->stride[0] != 1 || query_start->stride[0] != 1 ||
@@ -1019,6 +1020,7 @@ static int decode_weights(const forge_tensor* q, const forge_tensor* k_new, cons
   FORGE_TRY(check_qk_options(qk, q->shape[2]));
   FORGE_TRY(check_weights(weights, q->shape[0], k_cache->shape[1], true));
   if (plan.p.B == 0) return FORGE_OK;
+  FORGE_TRY(check_rows_apart(out, q->shape[2]));
   if (k_new) {
     FORGE_TRY(check_vec16(k_new, 2));
     FORGE_TRY(check_vec16(v_new, 2));
