@@ -805,14 +805,16 @@ namespace {
 // steps, stay below 2^31.
 constexpr int64_t kMaxLongBlocks = INT32_MAX / kBlockSize - 256;
 
+// Neighbouring elements along the last dimension (one alone has no neighbour).
+bool inner_stride_1(const forge_tensor* t) { return t->shape[t->ndim - 1] <= 1 || t->stride[t->ndim - 1] == 1; }
+
 // A device vector of n int32: contiguous.
 int check_i32_vector(const forge_tensor* t, int64_t n) {
   FORGE_TRY(check_tensor(t, FORGE_I32, 1));
   if (t->shape[0] != n) return FORGE_ERR_SHAPE;
   if (n == 0) return FORGE_OK;
   if (!t->data) return FORGE_ERR_NULL;
-  if (n > 1 && t->stride[0] != 1) return FORGE_ERR_SHAPE;
-  return FORGE_OK;
+  return inner_stride_1(t) ? FORGE_OK : FORGE_ERR_SHAPE;
 }
 
 // Scratch that the caller owns: `need` bytes, on a 256-byte boundary.
@@ -919,8 +921,8 @@ static int tree_attention(const forge_tensor* q, const forge_tensor* k_cache, co
   FORGE_TRY(check_rows_apart(out, D));
   if ((MB > 0 && !block_tables->data) || !context_lens->data || !query_start->data || !tree_mask->data)
     return FORGE_ERR_NULL;
-  if (block_tables->stride[1] != 1 || context_lens->stride[0] != 1 || query_start->stride[0] != 1 ||
-      tree_mask->stride[1] != 1)
+  if (!inner_stride_1(block_tables) || !inner_stride_1(context_lens) || !inner_stride_1(query_start) ||
+      !inner_stride_1(tree_mask))
     return FORGE_ERR_SHAPE;
   if (NB > 0 && (!k_cache->data || !v_cache->data)) return FORGE_ERR_NULL;
 
@@ -1109,7 +1111,7 @@ int forge_paged_evict_select(const forge_tensor* weights, const forge_tensor* co
   if (B > 65535 || Hkv > 65535 || kept->shape[2] > INT32_MAX) return FORGE_ERR_UNSUPPORTED;
   if (B == 0 || Hkv == 0) return FORGE_OK;
   if (!kept->data) return FORGE_ERR_NULL;
-  if (kept->stride[2] != 1) return FORGE_ERR_SHAPE;
+  if (!inner_stride_1(kept)) return FORGE_ERR_SHAPE;
   FORGE_TRY(check_rows_apart(kept, budget));
 
   int dev = 0, sms = 0;
@@ -1160,7 +1162,7 @@ int forge_paged_kv_compact(forge_tensor* k_cache, forge_tensor* v_cache, const f
   if (MB > 0 && !block_tables->data) return FORGE_ERR_NULL;
   if (K > 0 && !kept->data) return FORGE_ERR_NULL;
   if (NB > 0 && (!k_cache->data || !v_cache->data)) return FORGE_ERR_NULL;
-  if (block_tables->stride[1] != 1 || (K > 1 && kept->stride[2] != 1)) return FORGE_ERR_SHAPE;
+  if (!inner_stride_1(block_tables) || !inner_stride_1(kept)) return FORGE_ERR_SHAPE;
 
   int dev = 0, sms = 0;
   int* err = nullptr;
