@@ -159,8 +159,9 @@ FORGE_API int forge_paged_kv_append(const forge_tensor *k_new, const forge_tenso
  * Split scratch: a per-(device, stream) buffer that the library owns.  It is
  * allocated on first need and grown when a larger problem arrives, in stream
  * order on `stream` (cudaMallocAsync, zero-filled by cudaMemsetAsync; the old
- * buffer goes back with cudaFreeAsync after the work queued before it, unless
- * a captured call took it), so no call synchronises the host.  While `stream` is being captured into a CUDA
+ * buffer goes back with cudaFreeAsync after the work queued before it; one that
+ * graphs captured stays until a call on the stream finds them destroyed), so no
+ * call synchronises the host.  While `stream` is being captured into a CUDA
  * graph the scratch cannot grow: such a call returns FORGE_ERR_WORKSPACE
  * before enqueuing anything, so make the first call of the largest size on a
  * stream before capturing it.  Use forge_paged_gqa_decode_ex to pass
@@ -398,7 +399,7 @@ FORGE_API int forge_paged_prefill(const forge_tensor *q, const forge_tensor *k_c
  * They follow the conventions at the top of this file: asynchronous, no host
  * read of device memory, capturable, errors as statuses and device codes.
  * Scratch that a captured call took stays valid when a later call on its
- * stream needs more (the graph keeps the old one), but calls that share a
+ * stream needs more (the graph keeps the old one until it is destroyed), but calls that share a
  * stream's scratch must not overlap on the GPU: do not replay two graphs that
  * were captured on one stream at the same time, nor one beside that stream's
  * own calls.  The _ex forms take scratch that the caller owns instead, and

@@ -4,6 +4,7 @@
 // (no device reads, so calls stay asynchronous and capturable), the split
 // workspace cache, the device error word, and the kernel launches.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -11,6 +12,7 @@
 #include <memory>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 
@@ -39,11 +41,21 @@ int g_num_sms[kMaxDevices];
 // mutex is held from the lookup until the kernel that uses it is enqueued, so
 // a call that grows it (and releases the old buffer in stream order) never
 // runs between another call's lookup and launch on the same stream.
+//
+// A graph that captured a call replays into the buffer it captured.  Each such
+// graph holds a user object, whose destructor (when the graph and all of its
+// executables are gone) takes the graph off the buffer's count; a buffer that
+// is outgrown while graphs hold it waits in `retired` until none does.
+struct ScratchBuffer {
+  void* ptr = nullptr;
+  std::atomic<int>* graphs = nullptr;  // of its own, as long as the buffer; graphs that hold it
+};
 struct StreamScratch {
   std::mutex mu;
-  void* ptr = nullptr;
+  ScratchBuffer buf;
   size_t bytes = 0;
-  bool captured = false;  // a graph holds `ptr`: it is not freed when the scratch grows
+  unsigned long long capture_id = 0;   // the last capture that took `buf`
+  std::vector<ScratchBuffer> retired;
 };
 std::map<std::pair<int, cudaStream_t>, std::unique_ptr<StreamScratch>> g_workspaces;  // guarded by g_mu
 
@@ -395,46 +407,93 @@ int launch_plan(DecodePlan* plan, cudaStream_t stream) {
   return FORGE_OK;
 }
 
+void CUDART_CB graph_lets_go(void* graphs) { static_cast<std::atomic<int>*>(graphs)->fetch_sub(1); }
+
+// Puts the buffer into the count of a graph under capture, once per capture.
+int hold_for_graph(StreamScratch* sc, cudaGraph_t graph, unsigned long long id) {
+  if (sc->capture_id == id) return FORGE_OK;
+  cudaUserObject_t object;
+  if (cudaUserObjectCreate(&object, sc->buf.graphs, graph_lets_go, 1, cudaUserObjectNoDestructorSync) != cudaSuccess)
+    return FORGE_ERR_CUDA;
+  sc->buf.graphs->fetch_add(1);
+  if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+    cudaUserObjectRelease(object, 1);  // calls graph_lets_go
+    return FORGE_ERR_CUDA;
+  }
+  sc->capture_id = id;
+  return FORGE_OK;
+}
+
+// A larger buffer in the place of the one there, which is retired.
+int grow_scratch(StreamScratch* sc, size_t bytes, cudaStream_t stream) {
+  ScratchBuffer b;
+  try {
+    sc->retired.reserve(sc->retired.size() + 1);
+    b.graphs = new std::atomic<int>(0);
+  } catch (...) {
+    return FORGE_ERR_CUDA;  // out of host memory
+  }
+  cudaError_t e = cudaMallocAsync(&b.ptr, bytes, stream);
+  if (e == cudaSuccess) {
+    e = cudaMemsetAsync(b.ptr, 0, bytes, stream);
+    if (e != cudaSuccess) cudaFreeAsync(b.ptr, stream);
+  }
+  if (e != cudaSuccess) {
+    delete b.graphs;
+    return FORGE_ERR_CUDA;
+  }
+  if (sc->buf.ptr) sc->retired.push_back(sc->buf);
+  sc->buf = b;
+  sc->bytes = bytes;
+  sc->capture_id = 0;
+  return FORGE_OK;
+}
+
+// Frees, in stream order, the retired buffers that no graph holds any more.
+void give_back(StreamScratch* sc, cudaStream_t stream) {
+  for (size_t i = 0; i < sc->retired.size();) {
+    const ScratchBuffer& b = sc->retired[i];
+    if (b.graphs->load() == 0 && cudaFreeAsync(b.ptr, stream) == cudaSuccess) {
+      delete b.graphs;
+      sc->retired.erase(sc->retired.begin() + i);
+    } else {
+      ++i;
+    }
+  }
+}
+
 // Library-owned workspace for (device, stream), grown on demand with
 // stream-ordered allocation: the new buffer is allocated and zero-filled on
 // `stream` (the split arrival counters start at zero; kernels return them to
 // zero), and the old one is released with cudaFreeAsync on the same stream,
-// after the work already queued there.  No host synchronisation.  Growth is
-// refused while `stream` is being captured (the buffer would belong to the
-// graph).  On success `hold` owns the scratch's lock: the caller keeps it
-// until its kernel is enqueued.
+// after the work already queued there, once no graph holds it.  No host
+// synchronisation.  Growth is refused while `stream` is being captured (the
+// buffer would belong to the graph).  On success `hold` owns the scratch's
+// lock: the caller keeps it until its kernel is enqueued.
 int cached_workspace(int dev, cudaStream_t stream, size_t bytes, void** out, std::unique_lock<std::mutex>* hold) {
   StreamScratch* sc = nullptr;
-  {
+  try {
     std::lock_guard<std::mutex> lock(g_mu);
     auto& slot = g_workspaces[{dev, stream}];
     if (!slot) slot.reset(new StreamScratch);
     sc = slot.get();  // never removed, so the pointer stays valid
+  } catch (...) {
+    return FORGE_ERR_CUDA;  // out of host memory
   }
   std::unique_lock<std::mutex> lock(sc->mu);
-  if (sc->bytes < bytes) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return FORGE_ERR_CUDA;
-    if (cap != cudaStreamCaptureStatusNone) return FORGE_ERR_WORKSPACE;
-    void* p = nullptr;
-    if (cudaMallocAsync(&p, bytes, stream) != cudaSuccess) return FORGE_ERR_CUDA;
-    if (cudaMemsetAsync(p, 0, bytes, stream) != cudaSuccess) {
-      cudaFreeAsync(p, stream);
-      return FORGE_ERR_CUDA;
-    }
-    if (sc->ptr && !sc->captured && cudaFreeAsync(sc->ptr, stream) != cudaSuccess) {
-      cudaFreeAsync(p, stream);
-      return FORGE_ERR_CUDA;
-    }
-    sc->ptr = p;
-    sc->bytes = bytes;
-    sc->captured = false;
-  } else if (!sc->captured) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return FORGE_ERR_CUDA;
-    sc->captured = cap != cudaStreamCaptureStatusNone;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  cudaGraph_t graph = nullptr;
+  if (cudaStreamGetCaptureInfo(stream, &cap, &id, &graph, nullptr, nullptr, nullptr) != cudaSuccess)
+    return FORGE_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) {
+    if (sc->bytes < bytes) return FORGE_ERR_WORKSPACE;
+    if (cap == cudaStreamCaptureStatusActive) FORGE_TRY(hold_for_graph(sc, graph, id));
+  } else {
+    if (sc->bytes < bytes) FORGE_TRY(grow_scratch(sc, bytes, stream));
+    give_back(sc, stream);
   }
-  *out = sc->ptr;
+  *out = sc->buf.ptr;
   *hold = std::move(lock);
   return FORGE_OK;
 }
