@@ -483,21 +483,20 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
   // beside this one, and a non-coherent load wants unchanging data).
   griddep_wait();
   if (warp == 0) {
-    if (blockIdx.x == 0) {  // the rules for every sequence, checked once
-      int code = 0;
-      for (int b = lane; b < p.B; b += 32) {
-        const int s0 = p.query_start[b], s1 = p.query_start[b + 1], L = p.context_lens[b];
-        const int64_t n = static_cast<int64_t>(s1) - s0;
-        if (n < 0 || s1 > p.T || (b == 0 && s0 != 0)) code = kDevErrQuery;
-        if (n > 0 && (L < 0 || L > p.MB * kBlockSize))
-          code = kDevErrLength;
-        else if (n > L || n > 64ll * p.W)
-          code = n > 0 ? kDevErrQuery : code;
-      }
-      if (code) record_error(p.err, code);
-    }
     const Share sh = share_of<G, C::kItemRows>(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), lane);
     if (lane == 0) *share = sh;
+  } else if (warp == 1 && blockIdx.x == 0) {  // the rules for every sequence, checked once
+    int code = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const int s0 = p.query_start[b], s1 = p.query_start[b + 1], L = p.context_lens[b];
+      const int64_t n = static_cast<int64_t>(s1) - s0;
+      if (n < 0 || s1 > p.T || (b == 0 && s0 != 0)) code = kDevErrQuery;
+      if (n > 0 && (L < 0 || L > p.MB * kBlockSize))
+        code = kDevErrLength;
+      else if (n > L || n > 64ll * p.W)
+        code = n > 0 ? kDevErrQuery : code;
+    }
+    if (code) record_error(p.err, code);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -527,7 +526,6 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
       }
       __syncwarp();
     };
-    load_q();
     do {
       const int32_t* row = p.block_tables + static_cast<int64_t>(k.b) * p.bt_sb;
       // block ids of 8 stages: lane l holds block l % 4 of stage l / 4
@@ -536,6 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
         return jb * kBlockSize < k.s.L ? row[jb] : -1;
       };
       int ids = table_group(k.st0), ahead = k.st1 - k.st0 > 8 ? table_group(k.st0 + 8) : -1;
+      if (seg == 0) load_q();  // while the block ids are on their way
       for (int st = k.st0; st < k.st1; ++st, ++ring) {
         const int in = st - k.st0;
         if (in > 0 && in % 8 == 0) {
