@@ -1243,7 +1243,8 @@ int forge_paged_kv_compact(forge_tensor* k_cache, forge_tensor* v_cache, const f
   p.k_sh = kept->stride[1];
   p.kept_lens = static_cast<const int32_t*>(kept_lens->data);
   p.dst_start = dst_start ? static_cast<const int32_t*>(dst_start->data) : nullptr;
-  if (weights && weights->data) {
+  if (weights) {
+    p.totals = true;
     p.weights = static_cast<float*>(weights->data);
     p.w_sb = weights->stride[0];
     p.w_sh = weights->stride[1];

@@ -121,7 +121,8 @@ struct CompactParams {
   int64_t k_sb, k_sh;
   const int32_t* kept_lens;
   const int32_t* dst_start;  // null: 0
-  float* weights;            // null: none
+  bool totals;               // weights are given (of S columns, perhaps 0)
+  float* weights;
   int64_t w_sb, w_sh;
   int B, Hkv, NB, MB, D, K, S;
   int* err;

@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const CompactP
 template <int G>
 cudaError_t launch_acc(const WeightsParams& p, cudaStream_t stream) {
   const int64_t span = std::min<int64_t>(p.S, static_cast<int64_t>(p.MB) * kBlockSize);
-  const dim3 grid(static_cast<unsigned>((span + kAccTokens - 1) / kAccTokens), static_cast<unsigned>(p.Hkv),
+  // (one block where the totals have no columns: it records longer sequences)
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (span + kAccTokens - 1) / kAccTokens)), static_cast<unsigned>(p.Hkv),
                   static_cast<unsigned>(p.B));
   return launch_pdl(accumulate_weights_kernel<G>, grid, dim3(kAccThreads), 0, stream, p);
 }
@@ -553,7 +554,7 @@ cudaError_t launch_acc(const WeightsParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_accumulate_weights(const WeightsParams& p, int G, cudaStream_t stream) {
-  if (p.B == 0 || p.S == 0 || p.MB == 0) return cudaSuccess;
+  if (p.B == 0 || p.MB == 0) return cudaSuccess;
   switch (G) {
     case 1: return launch_acc<1>(p, stream);
     case 2: return launch_acc<2>(p, stream);
@@ -600,7 +601,7 @@ static cudaError_t launch_move(const CompactParams& p, int cluster, cudaStream_t
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kernel), kSmem, done);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(kernel,
-                            dim3(static_cast<unsigned>(p.Hkv) * cluster, static_cast<unsigned>(p.B), p.weights ? 3u : 2u),
+                            dim3(static_cast<unsigned>(p.Hkv) * cluster, static_cast<unsigned>(p.B), p.totals ? 3u : 2u),
                             cluster, dim3(kMoveThreads), kSmem, stream, p, cluster);
 }
 
