@@ -42,3 +42,109 @@ def test_totals_of_no_columns_are_reported():
     decode(a)
     binding.forge_paged_kv_compact(a["k"], a["v"], a["tables"], a["lens"], kept, n, weights=a["totals"])
     clean()
+
+
+# ---------------------------------------------------------------- lists and tables
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "same"])
+def test_lists_longer_than_a_cluster_holds(kind):
+    """More than 16 * 8192 positions: keys are read again from L2, and a thread's run is longer than 32."""
+    L = 16 * 8192 + 70001
+    x = totals_of(kind, (1, 2, (L + 3) // 4 * 4), 1)
+    check_select(x, [L], L // 2, 5, 1000)
+    check_select(x, [L], 77, 1, 2)
+
+
+def test_a_list_just_past_what_a_cluster_holds():
+    for L in (16 * 8192 + 5, 16 * 8192 + 6, 16 * 8192 + 16 * 1024):
+        check_select(totals_of("near", (1, 1, (L + 3) // 4 * 4), L), [L], 5000, 3, 2)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_cut_trees_of_many_sequences(out_dtype):
+    """More sequences than a warp, long enough to be cut, with empty ones among them."""
+    lens = [700 + 37 * i % 900 for i in range(70)]
+    nodes = [(3 * i) % 11 for i in range(70)]
+    check_tree(make_tree(lens, nodes, 2, 4, 64, out_dtype, seed=2))
+
+
+def wider(tables, width):
+    t = torch.full((tables.shape[0], width), -1, dtype=torch.int32, device=DEV)
+    t[:, :tables.shape[1]] = tables
+    return t
+
+
+@pytest.mark.parametrize("lens,nodes", [([600, 33, 1, 290], [9, 20, 1, 40]), ([20], [4])])
+def test_trees_in_tables_far_wider_than_the_lengths(lens, nodes):
+    a = make_tree(lens, nodes, 2, 4, 128, torch.bfloat16, seed=3)
+    a["tables"] = wider(a["tables"], 4096)
+    check_tree(a)
+
+
+@pytest.mark.parametrize("lens", [[600, 33, 1, 290, 0, 1100], [20]])
+def test_totals_in_tables_far_wider_than_the_lengths(lens):
+    a = make(lens, 2, 4, 128, torch.float32, seed=4, S=65536)
+    before = a["totals"].clone()
+    a["tables"] = wider(a["tables"], 4096)
+    ref, bound, tot, tb = plain.weights(a["q"], a["k"], a["v"], a["tables"], a["lens"], a["scale"], a["out"], a["totals"])
+    decode(a)
+    clean()
+    within(a["out"], ref, bound)
+    within(a["totals"], tot, tb)
+    for b, L in enumerate(lens):
+        assert torch.equal(a["totals"][b, :, L:], before[b, :, L:])
+    kept, n = torch.full((len(lens), 2, 64), -5, dtype=torch.int32, device=DEV), i32([-5] * len(lens))
+    binding.forge_paged_evict_select(a["totals"], a["lens"], 64, 4, 16, kept, n)
+    clean()
+    want = plain.select(a["totals"], lens, 64, 4, 16)
+    for b in range(len(lens)):
+        assert [kept[b, g, :n[b]].tolist() for g in range(2)] == want[b]
+
+
+# ---------------------------------------------------------------- decode with totals: values
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.5])
+@pytest.mark.parametrize("G", [1, 8])
+def test_totals_at_odd_scales(scale, G):
+    a = make([700, 33, 1], 2, G, 64, torch.float32, seed=5)
+    a["scale"] = scale
+    ref, bound, tot, tb = plain.weights(a["q"], a["k"], a["v"], a["tables"], a["lens"], scale, a["out"], a["totals"])
+    decode(a)
+    clean()
+    within(a["out"], ref, bound)
+    within(a["totals"], tot, tb)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("pos", [5, 650])
+def test_a_bad_value_stays_in_its_dim(bad, pos):
+    """An infinity or NaN of V reaches its own dim of its own KV head, and no total."""
+    a = make([700, 33], 2, 4, 128, torch.float32, seed=6)
+    ref, bound, tot, tb = plain.weights(a["q"], a["k"], a["v"], a["tables"], a["lens"], a["scale"], a["out"], a["totals"])
+    a["v"][int(a["tables"][0, pos // 16]), 1, pos % 16, 3] = bad
+    decode(a)
+    clean()
+    within(a["totals"], tot, tb)
+    hit = torch.zeros_like(a["out"], dtype=torch.bool)
+    hit[0, 4:8, 3] = True
+    got = a["out"].double()
+    assert not got[hit].isfinite().any()
+    assert ((got - ref).abs()[~hit] <= bound[~hit]).all()
+
+
+def test_what_follows_empty_sequences_waits_for_the_decode():
+    """Sequences that are all empty leave the totals' grid nothing to do; a copy behind the call must still find the
+    decode's zeros, in an output that has held something else until then."""
+    big = make([4000] * 40, 4, 4, 128, torch.float32, seed=12)
+    a = make([0] * 40, 4, 4, 128, torch.float32, seed=11, S=2048)
+    outs = [torch.full_like(a["out"], 7.25) for _ in range(20)]
+    seen = [torch.empty_like(a["out"]) for _ in outs]
+    totals = a["totals"].clone()
+    torch.cuda.synchronize()
+    for out, copy in zip(outs, seen):
+        decode(big)
+        a["out"] = out
+        decode(a)
+        copy.copy_(out)
+    clean()
+    assert all((x == 0).all() for x in seen) and torch.equal(a["totals"], totals)
