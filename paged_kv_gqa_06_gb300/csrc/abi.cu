@@ -1004,7 +1004,6 @@ static int tree_attention(const forge_tensor* q, const forge_tensor* k_cache, co
   p.o_st = out->stride[0];
   p.o_sh = out->stride[1];
   p.B = static_cast<int>(B);
-  p.Hq = static_cast<int>(Hq);
   p.Hkv = static_cast<int>(Hkv);
   p.NB = static_cast<int>(NB);
   p.MB = static_cast<int>(MB);

@@ -165,7 +165,7 @@ struct TreeParams {
   int64_t m_st;
   void* out;
   int64_t o_st, o_sh;
-  int B, Hq, Hkv, NB, MB, T, W;
+  int B, Hkv, NB, MB, T, W;
   float qk_scale_log2;
   int min_share;               // least length of a CTA's share of the work
   int split;                   // whether items may be cut
