@@ -399,11 +399,19 @@ FORGE_API int forge_paged_prefill(const forge_tensor *q, const forge_tensor *k_c
  * They follow the conventions at the top of this file: asynchronous, no host
  * read of device memory, capturable, errors as statuses and device codes.
  * Scratch that a captured call took stays valid when a later call on its
- * stream needs more (the graph keeps the old one until it is destroyed), but calls that share a
- * stream's scratch must not overlap on the GPU: do not replay two graphs that
- * were captured on one stream at the same time, nor one beside that stream's
- * own calls.  The _ex forms take scratch that the caller owns instead, and
- * keeps allocated as long as a graph that captured the call lives.
+ * stream needs more (the graph keeps the old one until it is destroyed), but
+ * calls that share a stream's scratch must not overlap on the GPU: do not
+ * replay two graphs that were captured on one stream at the same time, nor one
+ * beside that stream's own calls.  The _ex forms take scratch that the caller
+ * owns instead, and keeps allocated as long as a graph that captured the call
+ * lives.
+ * Only the decode adds weights to totals.  forge_paged_prefill leaves none: the
+ * totals of a prompt's tokens are what the caller put there (0) until decode
+ * steps have added to them, and a selection before that finds them equal and
+ * keeps the lowest positions.
+ * Split lengths, grids and scratch of the decode with totals and the selection
+ * go by the widths MB and S, not by the lengths, which only the device knows:
+ * tables and totals much wider than the longest sequence cost time.
  */
 
 /*
@@ -438,16 +446,16 @@ FORGE_API int forge_paged_prefill(const forge_tensor *q, const forge_tensor *k_c
  *                  range are left as they are.
  * D in {64, 128}, Hq / Hkv in {1, 2, 4, 8}.  A query_start or length that
  * breaks the rules is recorded as FORGE_DEVERR_QUERY / FORGE_DEVERR_LENGTH
- * and that sequence's rows are not written; a bad block id as
- * FORGE_DEVERR_BLOCK_ID (the rows are written, with that block's tokens
- * undefined).
+ * and that sequence's rows are not written (the length of one without nodes is
+ * not looked at); a bad block id as FORGE_DEVERR_BLOCK_ID (the rows are
+ * written, with that block's tokens undefined).
  *
  * Arithmetic: bf16 products with fp32 accumulation on the tensor cores,
  * softmax in fp32, the weights in the P V product as bf16 high + low parts
  * (about 16 significant bits; with f32 out a third part, 24 bits).  One sum on
  * the tensor cores takes at most 640 products of 16 tokens (384 with f32 out),
- * however long the context; sums are joined in fp32.  The result
- * depends on the inputs and the GPU's SM count alone: it repeats bit for bit.
+ * however long the context; sums are joined in fp32.  The result depends on
+ * the inputs and the GPU's SM count alone: it repeats bit for bit.
  * Enqueues one kernel, or two when contexts are long enough to be cut over the
  * SMs.  The cut rows live in the library-owned scratch of the stream (at most
  * about 80 MB; its growth, capture and thread-safety as for
@@ -504,7 +512,9 @@ FORGE_API int forge_paged_tree_attention_ex(const forge_tensor *q, const forge_t
  *                  FORGE_DEVERR_LENGTH and its totals past S are skipped.
  * Rows of `weights` must not overlap (FORGE_ERR_SHAPE): one of the two strides
  * is at least S, the other covers all of its steps; nor must rows of `out`.
- * With f32 out the P V product takes the weights at 24 bits, not 16.
+ * With f32 out the P V product takes the weights at 24 bits, not 16.  An
+ * infinite V element may give NaN in its dimension instead of an infinity; no
+ * total changes by it.
  * Scratch, its growth and thread-safety as in forge_paged_gqa_decode
  * (library-owned); it also holds the call's logits, B * Hq * MB * 16 * 4
  * bytes.  Enqueues two kernels.

@@ -134,9 +134,9 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 //
 // What bounds it: the latency of these steps and the instructions of their
 // scans; a list is tens of KB.  Wide digits and one CTA for lists of up to
-// 8192 keep the steps few.  256 lists of 512 to 8192 tokens: 13.5 us (24.8 us
+// 8192 keep the steps few.  256 lists of 512 to 8192 tokens: 13.7 us (24.8 us
 // with four 8-bit passes over clusters of two CTAs of 512 threads; 16.5 us
-// with 512 threads here); one of 32768 for each of 8 heads: 16 us over
+// with 512 threads here); one of 32768 for each of 8 heads: 16.7 us over
 // clusters of 8 (34 us while every CTA read all of the others' 2048 counters
 // and not the groups' sums first).
 constexpr int kSelThreads = 1024;
@@ -389,12 +389,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 // with asynchronous 16-byte copies, which hold no registers.  (With rows and
 // addresses in registers, 170 a thread let one CTA onto an SM: 248 us on 32
 // sequences of 512-8192 tokens cut to 1024, 114 us with one round at a time;
-// now 44.7 us, 6.0 TB/s.  The barrier's arrival orders nothing: the rows have
-// landed; one that released also waited for the last round's writes to reach
-// L2, 62 us instead of 40 on one list of 16383 over 8 CTAs.)  The ring's sizes,
-// that batch / one list of 16383 among short ones: 512 threads, 3 rounds of
-// 1024 chunks 44.2 / 28.5 us; 4 rounds 45.0 / 28.6; 2048 chunks, 2 or 3 rounds
-// 45.9 / 28.8 and 46.6 / 32.9; 256 threads 45.8 / 28.7.
+// now 44.4 us, 6.0 TB/s.)  The barrier's arrival is relaxed: the asynchronous
+// copies of the round are complete, their values lie in shared memory, and no
+// write can change what they read; an arrival that releases would also wait
+// for the last round's own writes to reach L2.  That batch / one list of 16383
+// among short ones: 44.4 / 28.9 us; released 48.0 / 37.3; released a round
+// ahead, with a fourth stage, 53.7 / 37.0.  The ring's sizes: 512 threads, 3
+// rounds of 1024 chunks 44.2 / 28.5 us; 2048 chunks, 2 or 3 rounds 45.9 / 28.8
+// and 46.6 / 32.9; 256 threads 45.8 / 28.7.
 constexpr int kMoveThreads = 512;
 constexpr int kMoveStages = 3;
 constexpr int kMoveChunks = 1024;   // 16-byte chunks of a round and CTA, at most
@@ -546,8 +548,8 @@ template <int G>
 cudaError_t launch_acc(const WeightsParams& p, cudaStream_t stream) {
   const int64_t span = std::min<int64_t>(p.S, static_cast<int64_t>(p.MB) * kBlockSize);
   // (one block where the totals have no columns: it records longer sequences)
-  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (span + kAccTokens - 1) / kAccTokens)), static_cast<unsigned>(p.Hkv),
-                  static_cast<unsigned>(p.B));
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (span + kAccTokens - 1) / kAccTokens)),
+                  static_cast<unsigned>(p.Hkv), static_cast<unsigned>(p.B));
   return launch_pdl(accumulate_weights_kernel<G>, grid, dim3(kAccThreads), 0, stream, p);
 }
 
@@ -606,7 +608,8 @@ static cudaError_t launch_move(const CompactParams& p, int cluster, cudaStream_t
 }
 
 // CTAs per list and plane: as many as leave each about eight rounds of the
-// longest list, while they are not far more than the SMs hold (4 each).
+// longest list; doubled while K's and V's CTAs are fewer than 8 to an SM (which
+// holds 4), so up to 16.
 // Measured with 1 / 2 / 4 / 8 / 16: 32 sequences cut to 1024 tokens 49.1 /
 // 45.7 / 47.0 / 57.4 / 95.6 us, one list of 16383 221 / 113 / 70 / 40 / 28 us.
 cudaError_t launch_kv_compact(const CompactParams& p, int num_sms, cudaStream_t stream) {

@@ -14,8 +14,8 @@
 // head; rows past the tree are computed and not stored, since an MMA takes
 // its time whatever M holds).  Measured on GB300 (152 SMs, copy peak 6766
 // GB/s): 32 sequences of 512-8192 tokens, trees of 5-24 nodes, 32 / 8 heads,
-// D 128: 115 us, 5.5 TB/s; 8 sequences of 512-4096, 64 nodes: 38.5 us, 500
-// TFLOP/s of Q K^T and P V (the MMAs issued are half as many again); one of
+// D 128: 113 to 117 us from GPU to GPU, 5.4 TB/s; 8 sequences of 512-4096, 64
+// nodes: 38 us, 508 TFLOP/s of Q K^T and P V (the MMAs issued are half as many again); one of
 // 32768 among three short ones, 13 nodes, fp32 out: 42 us, 3.4 TB/s.
 //
 // Work split.  An item is (sequence, KV head, group of rows); its length is
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<D, MODE>::kThreads, Cfg<D, MODE>::kPair ? 
           if (mine) {
             unsigned char* dst = sm + (v ? C::kV : C::kK) + slot * C::kStage + c * kTok * 128 + u * kBlockSize * 128;
             // K and V that one item alone reads make way in L2 for the pieces'
-            // rows (the batch above: 123 -> 115 us)
+            // rows (the batch above: 121.8 -> 116.2 us)
             if (k.s.groups == 1)
               tma_load_4d(dst, v ? &tmv : &tmk, c * 64, 0, k.g, e, full, once);
             else
