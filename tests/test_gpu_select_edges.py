@@ -148,3 +148,44 @@ def test_what_follows_empty_sequences_waits_for_the_decode():
         copy.copy_(out)
     clean()
     assert all((x == 0).all() for x in seen) and torch.equal(a["totals"], totals)
+
+
+def test_lengths_that_a_selection_has_just_written():
+    """kept_lens as the lengths of the calls right behind the selection and the move, which start while these run: every
+    call must see this step's lengths, not those of the step before."""
+    lens = [700, 120, 333, 64, 1024, 15]
+    a = make(lens, 4, 4, 128, torch.float32, seed=7, S=1024)
+    budgets, sets = [64, 700, 200, 31, 1000], []
+    k0, v0, t0 = a["k"].clone(), a["v"].clone(), a["totals"].clone()
+    kept = torch.zeros(6, 4, 1024, dtype=torch.int32, device=DEV)
+    n = torch.zeros(6, dtype=torch.int32, device=DEV)
+    tree_out = torch.zeros(12, 16, 128, device=DEV)
+    tree_q = a["q"].repeat_interleave(2, dim=0)
+    start, mask = i32(range(0, 13, 2)), torch.tensor([[1], [3]] * 6, dtype=torch.int64, device=DEV)
+
+    def step(budget, wait):
+        out = torch.empty_like(a["out"])
+        for x, y in ((a["k"], k0), (a["v"], v0), (a["totals"], t0)):
+            x.copy_(y)
+        calls = [lambda: binding.forge_paged_evict_select(a["totals"], a["lens"], budget, 4, 16, kept, n),
+                 lambda: binding.forge_paged_kv_compact(a["k"], a["v"], a["tables"], a["lens"], kept, n, weights=a["totals"]),
+                 lambda: binding.forge_paged_gqa_decode(a["q"], a["k"], a["v"], a["tables"], n, a["scale"], out),
+                 lambda: binding.forge_paged_tree_attention(tree_q, a["k"], a["v"], a["tables"], n, start, mask, a["scale"],
+                                                            tree_out),
+                 lambda: binding.forge_paged_gqa_decode_weights(a["q"], a["k"], a["v"], a["tables"], n, a["scale"], a["out"],
+                                                                a["totals"])]
+        for call in calls:
+            call()
+            if wait:
+                torch.cuda.synchronize()
+        return [x.clone() for x in (out, tree_out, a["out"], a["totals"], n)]
+
+    for budget in budgets:
+        sets.append(step(budget, True))
+        assert sets[-1][4].tolist() == [min(L, budget) for L in lens]
+    for _ in range(20):
+        for budget, want in zip(budgets, sets):
+            got = step(budget, False)
+            for x, y in zip(got, want):
+                assert torch.equal(x, y)
+    clean()
